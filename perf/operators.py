@@ -337,9 +337,10 @@ def _block_own(s):
 def _block_autograd(s):
     from row_normalization_rmsnorm_gb300 import autograd as A
     t = s["t"]
-    y, h = A.block_rms_norm(t["x"], t["r"], t["w_post"], t["w_pre"], gate=t["gate"],
-                            rows_per_gate=s["rows_per_gate"] or None, residual_scale=s["a"], block_scale=s["b"],
-                            eps=EPS, offset=s["offset"], checkpoint=None if s["ckpt"] == "none" else s["ckpt"])
+    gate = t["gate"][0] if s["gate"] == "channel" else t["gate"]
+    y, h = A.block_rms_norm(t["x"], t["r"], t["w_post"], t["w_pre"], gate=gate, rows_per_gate=s["rows_per_gate"] or None,
+                            residual_scale=s["a"], block_scale=s["b"], eps=EPS, offset=s["offset"],
+                            checkpoint=None if s["ckpt"] == "none" else s["ckpt"])
     leaves = {"dx": t["x"], "dr": t["r"], "dgate": t["gate"], "dw_post": t["w_post"], "dw_pre": t["w_pre"]}
     leaves = {k: v for k, v in leaves.items() if v is not None and v.requires_grad}
     outs = [(y, t.get("dy")), (h, t["dh"])] if s["pre"] else [(h, t["dh"])]
