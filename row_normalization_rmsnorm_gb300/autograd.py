@@ -290,11 +290,16 @@ class BlockRMSNormFunction(torch.autograd.Function):
     y = RMSNorm(h; w_pre).  Returns (y, h), y None without w_pre."""
 
     @staticmethod
-    def forward(ctx, x, residual, w_post, w_pre, gate, rows_per_gate, residual_scale, block_scale, eps, offset, fmt):
+    def forward(ctx, x, residual, w_post, w_pre, gate, rows_per_gate, residual_scale, block_scale, eps, offset, fmt,
+                kept=True):
         x2, r2 = _rows(x), _rows(residual)
         g2, R = _gate_rows(gate, x, rows_per_gate)
         post, pre = w_post is not None, w_pre is not None
         y, h = (torch.empty_like(x2) if pre else None), torch.empty_like(x2)
+        if not kept:   # no backward follows
+            B.norm_block_rms_fwd(x2, r2, w_post, w_pre, y, h, gate=g2, rows_per_gate=R, residual_scale=residual_scale,
+                                 block_scale=block_scale, offset=offset, eps=eps)
+            return (_shaped(y, x.shape) if pre else None), _shaped(h, x.shape)
         rs1, rs2 = (_stat(x2) if post else None), (_stat(x2) if pre else None)
         full = fmt == B.NORM_SAVED_FULL
         # x is needed for its norm's gradients and for the gate's; h for its norm's
@@ -318,7 +323,7 @@ class BlockRMSNormFunction(torch.autograd.Function):
         R, residual_scale, block_scale, offset, fmt, x_shape, r_shape = ctx.args
         need_x, need_r, need_post, need_pre, need_gate = ctx.needs_input_grad[:5]
         if dy is None and dh is None:
-            return (None,) * 11
+            return (None,) * 12
         if w_pre is not None and dy is None:
             dy = torch.zeros_like(dh)
         dy2, dh2 = (None if t is None else _rows(t) for t in (dy, dh))
@@ -336,7 +341,7 @@ class BlockRMSNormFunction(torch.autograd.Function):
                              rows_per_gate=R, saved_format=fmt, workspace=ws, residual_scale=residual_scale,
                              block_scale=block_scale, offset=offset)
         return (None if dx is None else _shaped(dx, x_shape), None if dr is None else _shaped(dr, r_shape), dw1, dw2,
-                None if dg is None else _shaped(dg, ctx.gate_shape), None, None, None, None, None, None)
+                None if dg is None else _shaped(dg, ctx.gate_shape), None, None, None, None, None, None, None)
 
 
 def rms_norm(x, weight, eps=1e-6, offset=0.0, in_place=False, checkpoint=None):
@@ -388,16 +393,10 @@ def block_rms_norm(x, residual, w_post=None, w_pre=None, gate=None, rows_per_gat
     one row per sequence; x's shape: per token), or [rows, N] with
     rows_per_gate.  checkpoint="e4m3" or "int8" keeps x and h for the backward in
     8 bits."""
-    fmt = _format(checkpoint)
-    if _kept(x, residual, w_post, w_pre, gate):
-        return BlockRMSNormFunction.apply(x, residual, w_post, w_pre, gate, rows_per_gate, residual_scale, block_scale,
-                                          eps, offset, fmt)
-    x2, r2 = _rows(x), _rows(residual)
-    g2, R = _gate_rows(gate, x, rows_per_gate)
-    y, h = (None if w_pre is None else torch.empty_like(x2)), torch.empty_like(x2)
-    B.norm_block_rms_fwd(x2, r2, w_post, w_pre, y, h, gate=g2, rows_per_gate=R, residual_scale=residual_scale,
-                         block_scale=block_scale, offset=offset, eps=eps)
-    return (None if y is None else _shaped(y, x.shape)), _shaped(h, x.shape)
+    # (always through the function: an input that carries a forward-mode tangent
+    # need not require a gradient, and is refused there)
+    return BlockRMSNormFunction.apply(x, residual, w_post, w_pre, gate, rows_per_gate, residual_scale, block_scale, eps,
+                                      offset, _format(checkpoint), _kept(x, residual, w_post, w_pre, gate))
 
 
 class RMSNorm(torch.nn.Module):
