@@ -48,15 +48,20 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     if t.dim() == 0:
         raise ValueError("expected at least one dimension")
     if t.dim() == 2 and t.is_contiguous():
-        return t
-    if t.stride(-1) != 1:
-        t = t.contiguous()
-    try:
-        r = t.view(-1, t.shape[-1])
-    except RuntimeError:
-        return t.contiguous().view(-1, t.shape[-1])
-    # rows that share memory (a gradient expanded over the rows) are copied out
-    return r.contiguous() if r.shape[0] > 1 and r.stride(0) < r.shape[1] else r
+        r = t
+    else:
+        if t.stride(-1) != 1:
+            t = t.contiguous()
+        try:
+            r = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            return t.contiguous().view(-1, t.shape[-1])
+    rows, n = r.shape
+    if rows == 0 or r.stride(0) >= n:
+        return r
+    # rows that share memory (a gradient expanded over the rows) are copied out;
+    # the stride of a single row says nothing: it gets the row's length
+    return r.contiguous() if rows > 1 else r.as_strided((1, n), (n, 1))
 
 
 def _shaped(t, shape):
