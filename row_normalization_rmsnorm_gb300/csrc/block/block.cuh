@@ -1321,7 +1321,9 @@ int launch_block(Fn plain, Fn split, BlockCta cta, std::initializer_list<BlockSh
       // slice's scales start and end on 16 bytes
       if (ncl > 1 && q8 && NL % (qx ? 16 * kCkptGroup : kCkptGroup)) continue;
     } else {
-      NL = ncl == 1 ? p.N : ((p.N + ncl - 1) / ncl + 511) / 512 * 512;
+      // slices in whole warps of columns; as above where a checkpoint is read
+      const int unit = qx ? 16 * kCkptGroup : 32;
+      NL = ncl == 1 ? p.N : ((p.N + ncl - 1) / ncl + unit - 1) / unit * unit;
       if (NL * (ncl - 1) >= p.N) continue;
     }
     if (NL > kSliceCols) continue;
