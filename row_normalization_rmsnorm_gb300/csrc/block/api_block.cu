@@ -476,6 +476,7 @@ int norm_block_rms_bwd(const void* dy, int64_t dy_stride, const void* dh_out, in
       set_stream(p, SR, mdh, es);
       set_stream(p, SX, mx, q8 ? 1 : es);
       set_stream(p, SH, mh, q8 ? 1 : es);
+      p.room_x = gate != nullptr;   // x is read for its norm's gradients, else for the gate's alone
       if (streamed) {
         set_stream(p, SG, mg, es);
       } else {
@@ -516,7 +517,9 @@ int norm_block_rms_bwd(const void* dy, int64_t dy_stride, const void* dh_out, in
     // (8192 x 5120, a scale per channel: 2 us less than in two); without, the
     // weights' by the column reduction of the other norms, whose cluster form is
     // faster with many partial rows (backward 8192 x 2048: 45.2 against 49.0 us).
-    // Which one does not depend on the gradients wanted, so their bits do not.
+    // Neither which one nor the launch shape (room_x) depends on the gradients
+    // wanted, so their bits do not (unless one of them, or the x read for it alone,
+    // is all that is off 16 bytes: that takes the general form).
     const bool sum_gate = dgate && !streamed;
     if (!sum_gate) p.n_gates = 0;
     if (sum_gate || (gate && !streamed && (dw_post || dw_pre)))

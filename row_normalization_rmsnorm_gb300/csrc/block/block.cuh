@@ -1343,14 +1343,18 @@ int launch_block(Fn plain, Fn split, BlockCta cta, std::initializer_list<BlockSh
     }
     const int threads = (int)((NL + 32 * cols - 1) / (32 * cols)) * 32;
     p.part = (int)NL;
+    // a stage, and the room (`off`) that the shape is chosen by
     uint32_t off = 0;
+    p.stage_bytes = 0;
     for (int s = 0; s < kBlockStreams; ++s) {
-      p.soff[s] = off;
-      if (!p.in[s]) continue;
-      if (qx && (s == SX || s == SH)) off += (uint32_t)((NL + 15) / 16 * 16 + (NL + 511) / 512 * 16);
-      else off += ALN ? (uint32_t)(NL * es) : (uint32_t)((NL * es + 15) / 16 * 16 + 16);
+      p.soff[s] = p.stage_bytes;
+      if (!p.in[s] && !(s == SX && p.room_x)) continue;
+      uint32_t len;
+      if (qx && (s == SX || s == SH)) len = (uint32_t)((NL + 15) / 16 * 16 + (NL + 511) / 512 * 16);
+      else len = ALN ? (uint32_t)(NL * es) : (uint32_t)((NL * es + 15) / 16 * 16 + 16);
+      off += len;
+      if (p.in[s]) p.stage_bytes += len;
     }
-    p.stage_bytes = off;
     const void* fp = reinterpret_cast<const void*>(fn);
     const KernelInfo ki = kernel_info(fp, di);
     if (ki.max_dyn < 0) return NORM_ERR_CUDA;
@@ -1365,30 +1369,38 @@ int launch_block(Fn plain, Fn split, BlockCta cta, std::initializer_list<BlockSh
       const int64_t per_sm = (di.max_partial_rows * ncl + di.sms - 1) / di.sms;
       if (per_sm >= 1 && ctas > per_sm) ctas = (int)per_sm;
     }
-    int S = 0;
+    // the deepest ring of stages of `bytes` that leaves room for n CTAs an SM: its
+    // stages (0: not two) and shared memory
     size_t smem = 0;
-    for (; ctas >= 1; --ctas) {
-      size_t room = (size_t)di.smem_per_sm / ctas;
+    auto ring = [&](uint32_t bytes, int n) {
+      const size_t two = kBlockHeader + 2 * (size_t)bytes;
+      size_t room = (size_t)di.smem_per_sm / n;
       const size_t fixed_sm = (size_t)di.smem_reserved + 1536;   // reserved, and the static arrays
       room = room > fixed_sm ? room - fixed_sm : 0;
       if (room > (size_t)ki.max_dyn) room = (size_t)ki.max_dyn;
-      if (ctas > 1 && room < least) continue;
-      if (room < least) room = least;
-      S = (int)((room - kBlockHeader) / off);
+      if (n > 1 && room < two) return 0;
+      if (room < two) room = two;
+      int S = (int)((room - kBlockHeader) / bytes);
       const size_t inflight = (size_t)(di.tune_inflight_16k > 0 ? di.tune_inflight_16k : kInflightUnits) * 16384;
-      const int cap = 1 + (int)(inflight / ((size_t)ctas * off));
+      const int cap = 1 + (int)(inflight / ((size_t)n * bytes));
       if (S > cap) S = cap > 2 ? cap : 2;
       if (S > kBlockMaxStages) S = kBlockMaxStages;
       if (di.tune_max_stages >= 2 && S > di.tune_max_stages) S = di.tune_max_stages;
       for (; S >= 2; --S) {
-        smem = kBlockHeader + (size_t)S * off;
+        smem = kBlockHeader + (size_t)S * bytes;
         const int fit = cached_occupancy(fp, di, threads, smem);
-        if (fit < 0) return NORM_ERR_CUDA;
-        if (fit >= ctas) break;
+        if (fit < 0) return -1;
+        if (fit >= n) return S;
       }
+      return 0;
+    };
+    int S = 0;
+    for (; ctas >= 1; --ctas) {
+      S = ring(off, ctas);
+      if (S < 0) return NORM_ERR_CUDA;
       if (S >= 2) break;
     }
-    if (ctas < 1 || S < 2) continue;
+    if (ctas < 1) continue;
     // row groups resident at once, held to the rows and the partial rows
     int64_t G = (int64_t)di.sms * ctas;
     if (ncl > 1) {
@@ -1396,6 +1408,10 @@ int launch_block(Fn plain, Fn split, BlockCta cta, std::initializer_list<BlockSh
       if (G < 0) return NORM_ERR_CUDA;
       if (G == 0) continue;
     }
+    // (room that no stream takes deepens the ring: 4096 x 4096 fp32 with a frozen
+    // gate per token, three stages in place of two, 80 -> 69 us)
+    if (p.stage_bytes < off) S = ring(p.stage_bytes, ctas);
+    if (S < 2) return NORM_ERR_CUDA;
     if (G > p.M) G = p.M;
     if (acc && G > di.max_partial_rows) G = di.max_partial_rows;
     // a group counts its rows in 32 bits

@@ -15,8 +15,9 @@ enum BlockStream : int { SX = 0, SR = 1, SG = 2, SDY = 3, SH = 4, kBlockStreams 
 struct BlockParams {
   const char* in[kBlockStreams];     // null = absent
   int64_t in_stride[kBlockStreams];  // bytes between rows
-  uint32_t soff[kBlockStreams];      // offset in a stage (aligned-row kernels)
+  uint32_t soff[kBlockStreams];      // offset in a stage
   uint32_t stage_bytes;
+  int room_x;                        // the launch shape counts x's stream, read or not
   int part;                          // columns of a slice when a row is split
   int64_t min_stride;                // smallest in_stride of the rows of the activations' type
   // outputs: h and y (forward), the gradients of the residual and of x
