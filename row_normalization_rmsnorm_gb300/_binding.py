@@ -221,6 +221,7 @@ def _device(x, *others):
     for name, t in others:
         if t is None:
             continue
+        _tensor(t, name)
         if not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor (this library has no CPU path)")
         if t.get_device() != dev:
@@ -461,6 +462,11 @@ def _quick_vecs(dev, n, dtype, *tensors):
     return True
 
 
+def _on_dev(t, dev):
+    """Whether t is None or a tensor on that device."""
+    return t is None or (isinstance(t, torch.Tensor) and t.get_device() == dev)
+
+
 def _quick(x):
     """(device, M, N) of a 2-D CUDA tensor with rows, or None."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2 or x.dtype not in DTYPE_CODE:
@@ -509,7 +515,7 @@ def _quick_norm(x, w, rows, stats, ckpt, workspace, cols=()):
         if t is not None and (not isinstance(t, torch.Tensor) or not _quick_vecs(dev, N, t.dtype, t)
                               or (t.dtype is not wdt and t.dtype is not torch.float32)):
             return None
-    if any(t is None for t in rows[:1] + rows[-1:]) or (workspace is not None and workspace.get_device() != dev):
+    if any(t is None for t in rows[:1] + rows[-1:]) or not _on_dev(workspace, dev):
         return None
     sq = _quick_rows(dev, (M, _ckpt_bytes(N)), torch.uint8, ckpt)
     return None if sq is None else (dev, M, N, dt, wdt, st, sq[0])
@@ -794,17 +800,14 @@ def norm_block_rms_bwd(dy, dh_out, x, h, w_post, w_pre, rstd_post, rstd_pre, dx=
     full = saved_format == NORM_SAVED_FULL
     q = _quick_block(first, w_post, w_pre, (dy, dh_out, x, h, dx, dresidual) if full else (dy, dh_out, dx, dresidual),
                      (rstd_post, rstd_pre), () if full else (x, h), gate, rows_per_gate)
-    dgstride = 0
-    if dgate is not None and gate is not None:
-        dgstride = dgate.stride(0) if dgate.dim() == 2 else dgate.shape[-1]
     if q is not None and (
             (dy is None) != (w_pre is None) or (dh_out is None and w_pre is None)
             or (x is None and (w_post is not None or dgate is not None)) or (h is None and w_pre is not None)
             or (rstd_post is None and w_post is not None) or (rstd_pre is None and w_pre is not None)
-            or (dgate is not None and (gate is None or dgate.shape != gate.shape or dgate.dtype is not gate.dtype
-                                       or dgate.stride(-1) != 1 or dgate.get_device() != q[0]))
+            or (dgate is not None and (gate is None or not _on_dev(dgate, q[0]) or dgate.shape != gate.shape
+                                       or dgate.dtype is not gate.dtype or dgate.stride(-1) != 1))
             or not _quick_vecs(q[0], q[2], q[4], dw_post, dw_pre)
-            or (workspace is not None and workspace.get_device() != q[0])):
+            or not _on_dev(workspace, q[0])):
         q = None   # wrong or unusual: the checks below say which
     if q is not None:
         dev, M, N, dt, wdt, st, sq, (grows, gstride, R, gdt) = q
@@ -837,6 +840,7 @@ def norm_block_rms_bwd(dy, dh_out, x, h, w_post, w_pre, rstd_post, rstd_pre, dx=
         if dgate is not None:
             if gate is None:
                 raise ValueError("dgate is given without a gate")
+            _tensor(dgate, "dgate")
             if tuple(dgate.shape) != tuple(gate.shape) or dgate.dtype != gate.dtype:
                 raise ValueError(f"dgate must have gate's shape {tuple(gate.shape)} and dtype {gate.dtype}, got "
                                  f"{tuple(dgate.shape)}, {dgate.dtype}")
@@ -847,6 +851,7 @@ def norm_block_rms_bwd(dy, dh_out, x, h, w_post, w_pre, rstd_post, rstd_pre, dx=
                       ("dresidual", dresidual), ("dgate", dgate), ("dw_post", dw_post), ("dw_pre", dw_pre),
                       ("workspace", workspace))
         sdy, sdh, sx, sh, sdx, sdr = _rs(dy), _rs(dh_out), _rs(x), _rs(h), _rs(dx), _rs(dresidual)
+    dgstride = 0 if dgate is None else dgate.stride(0) if dgate.dim() == 2 else dgate.shape[-1]
     wsp, wsb = _ws(workspace)
     _on(dev, lambda: _check("norm_block_rms_bwd", lib.norm_block_rms_bwd(
         _ptr(dy), sdy, _ptr(dh_out), sdh, _ptr(x), sx, _ptr(h), sh, int(saved_format), _ptr(w_post), _ptr(w_pre),
