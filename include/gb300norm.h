@@ -261,7 +261,8 @@ GB300NORM_API int norm_rms_bwd_noalloc(const void *dy, int64_t dy_stride,
  * value.  Buffers and strides (in BYTES, at least that many) must be multiples
  * of 16.
  *   encode: x [M, x_stride] of dtype -> ckpt;  decode: ckpt -> x, rounded once
- *   to dtype.  Neither may overlap.  M == 0 is a successful no-op.
+ *   to dtype (a value whose code stands for more than dtype holds, such as 65504
+ *   in e4m3 for 65536 in fp16, becomes infinite).  Neither may overlap.  M == 0 is a successful no-op.
  */
 GB300NORM_API int norm_ckpt_row_bytes(int64_t N, size_t *bytes);
 GB300NORM_API int norm_ckpt_encode(const void *x, int64_t x_stride, void *ckpt, int64_t ckpt_stride, int format,

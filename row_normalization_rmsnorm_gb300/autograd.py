@@ -10,7 +10,8 @@ which nothing requires grad saves nothing for a backward.
 All arithmetic runs in the library's kernels; this module allocates the
 outputs (and the dW / dB workspace) with torch and marshals arguments.
 Inputs may have any leading shape; the last dimension is normalised and
-must be contiguous.
+must be contiguous.  Forward-mode tangents are refused, and so are second
+derivatives through the checkpointed forms and the block boundary.
 """
 from __future__ import annotations
 

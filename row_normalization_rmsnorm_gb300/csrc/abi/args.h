@@ -13,7 +13,8 @@ namespace gb300norm {
 // word.  Defined in api.cu.
 int get_device(DevInfo* out, int** status);
 
-// Test hook: 1 = the aligned-row kernels withhold each row group's last copy.
+// Test hook: 1 = the kernels whose rows come by bulk copies withhold each row
+// group's last one.
 int hold_last_hook();
 
 inline int elem_size(int dt) {

@@ -1318,7 +1318,8 @@ int launch_block(Fn plain, Fn split, BlockCta cta, std::initializer_list<BlockSh
       if ((p.N / vec) % ncl) continue;
       NL = p.N / ncl;
       // a checkpoint's groups lie within a slice; where it is read (qx), a
-      // slice's scales start and end on 16 bytes
+      // slice's scales start and end on 16 bytes.  (Lengths that are not so split
+      // take the general form: backward 4096 x 13824 342 us, 4096 x 16384 175.)
       if (ncl > 1 && q8 && NL % (qx ? 16 * kCkptGroup : kCkptGroup)) continue;
     } else {
       // slices of what a warp takes at 16 columns a lane (a checkpoint that is read
