@@ -301,11 +301,13 @@ class BlockRMSNormFunction(torch.autograd.Function):
         x2, r2 = _rows(x), _rows(residual)
         g2, R = _gate_rows(gate, x, rows_per_gate)
         post, pre = w_post is not None, w_pre is not None
+        if not kept:   # no backward follows; outputs that are no views may be written over
+            y, h = (x2.new_empty(x.shape) if pre else None), x2.new_empty(x.shape)
+            B.norm_block_rms_fwd(x2, r2, w_post, w_pre, _shaped(y, x2.shape) if pre else None, _shaped(h, x2.shape),
+                                 gate=g2, rows_per_gate=R, residual_scale=residual_scale, block_scale=block_scale,
+                                 offset=offset, eps=eps)
+            return y, h
         y, h = (torch.empty_like(x2) if pre else None), torch.empty_like(x2)
-        if not kept:   # no backward follows
-            B.norm_block_rms_fwd(x2, r2, w_post, w_pre, y, h, gate=g2, rows_per_gate=R, residual_scale=residual_scale,
-                                 block_scale=block_scale, offset=offset, eps=eps)
-            return (_shaped(y, x.shape) if pre else None), _shaped(h, x.shape)
         rs1, rs2 = (_stat(x2) if post else None), (_stat(x2) if pre else None)
         full = fmt == B.NORM_SAVED_FULL
         # x is needed for its norm's gradients and for the gate's; h for its norm's

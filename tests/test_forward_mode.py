@@ -62,3 +62,17 @@ def test_a_call_without_gradients_keeps_nothing(ag, ck, monkeypatch):
         assert all(t is None for t in a[6:8])                       # the statistics
         assert kw.get("x_ckpt") is None and kw.get("h_ckpt") is None and not kw.get("ckpt_format", 0)
     assert ag.block_rms_norm(x, x, w, None)[0] is None
+
+
+@pytest.mark.parametrize("shape", [(4, N), (2, 2, N), (N,)])
+@pytest.mark.parametrize("i", [0, 1])
+def test_outputs_without_gradients_may_be_written_over(ag, shape, i):
+    """With what requires a gradient, too: they are no views."""
+    x, w, p = torch.randn(shape), torch.ones(N), torch.ones(N, requires_grad=True)
+    for keep_graph in (True, False):
+        with torch.set_grad_enabled(keep_graph):
+            o = ag.block_rms_norm(x, x, w, w)[i]
+        assert o.shape == shape and o.is_contiguous()
+        o.add_(p)
+        o.sum().backward()
+    assert torch.equal(p.grad, torch.full((N,), 2.0 * x.numel() / N))
